@@ -65,7 +65,9 @@ __device__ __forceinline__ void with_act(int act, const F& f) {
         f(std::integral_constant<int, GELU>{});
 }
 
-// fp8 operands' scales: one per token, one per weight row.
+// fp8 operands' scales: one per token, one per weight row.  A sum takes one
+// after the other: their product may be outside fp32's range where the value
+// is not.
 struct Scales {
     const float *x, *gate, *up;
 };
@@ -107,8 +109,8 @@ __global__ void __launch_bounds__(kThreads) gated_up_kernel(const void* xp, cons
                     const float sx = m0 + row < m ? sc.x[m0 + row] : 0.f;
 #pragma unroll
                     for (int t = 0; t < 8; ++t) {
-                        g[t] *= sx * (col < f ? sc.gate[col + t] : 0.f);
-                        u[t] *= sx * (col < f ? sc.up[col + t] : 0.f);
+                        g[t] = g[t] * sx * (col < f ? sc.gate[col + t] : 0.f);
+                        u[t] = u[t] * sx * (col < f ? sc.up[col + t] : 0.f);
                     }
                 }
 #pragma unroll
@@ -289,8 +291,8 @@ __global__ void __launch_bounds__(64 * WAVES) thin_up_kernel(const char* xp, con
         const int r = e >> 3, c = e & 7;
         float g = join.sum(r, c), u = join.sum(r, 8 + c);
         if constexpr (FP8) {
-            g *= sc.x[r] * sc.gate[n0 + c];
-            u *= sc.x[r] * sc.up[n0 + c];
+            g = g * sc.x[r] * sc.gate[n0 + c];
+            u = u * sc.x[r] * sc.up[n0 + c];
         }
         const int64_t at = (int64_t)r * f + n0 + c;
         h[at] = thin::to_bf16((act == SILU ? act_value<SILU>(g) : act_value<GELU>(g)) * u);
@@ -333,8 +335,8 @@ __global__ void __launch_bounds__(256) join_up_kernel(const float* part, int sha
     if constexpr (FP8) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            g[t] *= sc.x[row] * sc.gate[col + t];
-            u[t] *= sc.x[row] * sc.up[col + t];
+            g[t] = g[t] * sc.x[row] * sc.gate[col + t];
+            u[t] = u[t] * sc.x[row] * sc.up[col + t];
         }
     }
     with_act(act, [&](auto a) __attribute__((always_inline)) {
