@@ -1,5 +1,5 @@
 // dense_pick.h -- which tile shape a product of the tile engine takes, from
-// its sizes alone.  Host code.
+// its sizes alone.  Plain C++.
 //
 // Each shape's time is modelled as rounds of workgroups over the compute
 // units, a round costing a start-and-end part plus a part per K tile (128
@@ -12,7 +12,6 @@
 //   4096 x 1024 -> 2048:  128 x 128 (2 stages) 21.9 us, 256 x 256 26.0, 64 x 64 29.6
 //   8192 x 1024 -> 2048:  256 x 256 31.0 us, 128 x 128 36.4, 64 x 64 59.6
 #pragma once
-#include <hip/hip_runtime.h>
 #include <stdint.h>
 
 namespace dmm {
@@ -25,36 +24,28 @@ enum Tile {
     kTile64     // 64 rows x 64 columns (or x 64 columns of each of two matrices), four stages
 };
 
-// Compute units, of the device that is current at the first call: the choices
-// below are asked for several times a call, and all gfx950 devices of a process
-// have the same number.  A wrong one would only cost time.
-inline int device_units() {
-    static const int units = [] {
-        int dev = 0, v = 0;
-        if (hipGetDevice(&dev) != hipSuccess ||
-            hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v <= 0)
-            v = 256;
-        return v;
-    }();
-    return units;
-}
+// Compute units of the part this library is built for.  A constant and not the
+// device's property: a workspace query makes no HIP call, and the choices, with
+// them the workspace and the order of a call's sums, depend on the problem
+// alone.  On a device of fewer units a wrong choice costs time only.
+constexpr int kUnits = 256;
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
 
 // Time of t 64 x 64 tiles beside others in the same launch, and alone.
 inline double cost64_more(int64_t t, int64_t kt) {
-    return (double)t / (double)device_units() * (0.8 + 0.19 * (double)kt);
+    return (double)t / (double)kUnits * (0.8 + 0.19 * (double)kt);
 }
 inline double cost64(int64_t t, int64_t kt) {
-    return 2.7 + cost64_more(t < device_units() ? device_units() : t, kt);
+    return 2.7 + cost64_more(t < kUnits ? kUnits : t, kt);
 }
 
 // rows x cols output (count matrices of them in one launch), kt K tiles.
 // gated: a tile's columns are half of each of two matrices.
 // cost: where to put the modelled microseconds.
 inline Tile pick_tile(int64_t rows, int64_t cols, int64_t kt, bool gated, int count = 1, double* cost = nullptr) {
-    const int64_t cus = device_units();
+    constexpr int64_t cus = kUnits;
     const int64_t t256 = count * ceil_div(rows, 256) * ceil_div(cols, gated ? 128 : 256);
     const int64_t t128 = count * ceil_div(rows, 128) * ceil_div(cols, gated ? 64 : 128);
     const int64_t t64 = count * ceil_div(rows, 64) * ceil_div(cols, 64);

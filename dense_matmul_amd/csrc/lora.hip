@@ -414,7 +414,7 @@ static hipError_t launch_shrink_as(Shrink p, const split::Args* base, hipStream_
     // one launch where the first product's workgroups take one place on each
     // unit at most; more of them are held up by the stages they do not use
     // (256 tokens x 4096, 32 adapters of rank 16: 52 us against 42)
-    if (base && blocks <= device_units()) {
+    if (base && blocks <= kUnits) {
         split::Args b = *base;
         const int more = split::partial_blocks<C>(b);
         hipLaunchKernelGGL((shrink_and_base_kernel<MB, C>), dim3(blocks + more), dim3(kThreads), 0, st, p, blocks, b);
@@ -472,7 +472,7 @@ constexpr int kJoinMost = 256;  // tokens whose adapters' part is summed value b
 // How the shared product of few tokens is shared out.
 static split::Plan base_plan(int m, int n, int k) {
     const int64_t kt = ceil_div(k, 64);
-    const double one = (double)ceil_div(ceil_div(m, 64) * ceil_div(n, 64), device_units()) * (2.7 + 0.23 * (double)kt);
+    const double one = (double)ceil_div(ceil_div(m, 64) * ceil_div(n, 64), kUnits) * (2.7 + 0.23 * (double)kt);
     return split::plan(m, n, kt, 1, false, one);
 }
 
@@ -480,7 +480,7 @@ static split::Plan base_plan(int m, int n, int k) {
 // four K tiles at least to a share.
 static split::Plan shrink_plan(int m, int k, int r) {
     const int64_t kt = ceil_div(k, 64), tiles = ceil_div(m, 64) * ceil_div(r, 64);
-    int64_t s = 2 * device_units() / tiles;
+    int64_t s = 2 * kUnits / tiles;
     s = s > kt / 4 ? kt / 4 : s;
     s = s < 1 ? 1 : s > split::kMost ? split::kMost : s;
     const int64_t per = ceil_div(kt, s);

@@ -25,7 +25,7 @@ struct Plan {
 // = 1 where no split pays.  Model as in pick_tile: the tiles' round, the shares'
 // way to memory and back, and a second launch.
 inline Plan plan(int64_t rows, int64_t cols, int64_t kt, int segs, bool gated, double unsplit) {
-    const int64_t cus = device_units(), tiles = ceil_div(rows, 64) * ceil_div(cols, 64);
+    const int64_t cus = kUnits, tiles = ceil_div(rows, 64) * ceil_div(cols, 64);
     Plan best{1, (int)kt, segs};
     double c = unsplit;
     for (int64_t s = 2 / segs; s * segs <= kMost; ++s) {

@@ -223,7 +223,8 @@ dmm_status gemm_bf16_tile(const uint16_t* a, const uint16_t* b, uint16_t* c, int
  * batch may be empty (rows or m = 0: nothing is read, outputs that do not
  * depend on the batch's size are written as the empty sum, and pointers to
  * empty arrays may be NULL), and operands may exceed 2^31 bytes (one row of
- * a matrix may have at most 2^21 elements). */
+ * a matrix may have at most 2^21 elements).  The _workspace queries make no HIP
+ * call: a size depends on the arguments alone. */
 
 enum { DMM_BF16 = 0, DMM_FP32 = 1 };
 enum {
