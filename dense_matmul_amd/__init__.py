@@ -376,7 +376,13 @@ def _dims(t, name, dims, dtypes):
     raise ValueError(f"{name}: expected one of {', '.join(map(str, dtypes))}, got {t.dtype}")
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The current stream's handle of a device: in one step where this torch has the
+# call for it (private, so it may not), 0.05 us against 1.1.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+
+    def _raw_stream(dev):
+        return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _act(act):
