@@ -399,39 +399,26 @@ static hipError_t launch_up_as(const void* x, const void* wg, const void* wu, co
     return hipGetLastError();
 }
 
-// Tokens that take the thin kernels.
-constexpr int kThinMost = 16;
-
-template <bool FP8>
-static split::Plan up_plan(int m, int d, int f) {
-    double unsplit;
-    const int64_t kt = ceil_div(d * (FP8 ? 1 : 2), 128);
-    pick_tile(m, f, kt, true, 1, &unsplit);
-    return m <= kThinMost ? split::Plan{1, 0, 1} : split::plan(m, f, kt, 1, true, unsplit);
-}
-
 template <bool FP8>
 static hipError_t launch_up(const void* x, const void* wg, const void* wu, const Scales& sc, uint16_t* gate,
                             uint16_t* up, uint16_t* h, float* part, int m, int d, int f, int act, hipStream_t st) {
-    if (m <= kThinMost) {
-        const int kb = d * (FP8 ? 1 : 2);
-        if constexpr (FP8)
-            return THIN_BY_SIZE(launch_thin_up_fp8, m, kb, x, wg, wu, sc, gate, up, h, m, d, f, act, st);
-        else
-            return THIN_BY_SIZE(launch_thin_up, m, kb, x, wg, wu, sc, gate, up, h, m, d, f, act, st);
-    }
+    constexpr int E = FP8 ? 1 : 2;
     constexpr int S = FP8 ? 2 : 4;  // the fp8 steps alternate two fragment sets, so two stages
     using C64 = Cfg<64, 128, S, KC, KC, true, false, FP8>;
-    const split::Plan plan = up_plan<FP8>(m, d, f);
-    if (plan.shares > 1) {
-        const hipError_t e =
-            split::launch_partial<C64>({{x, x}, {wg, wu}, part, m, f, d * (FP8 ? 1 : 2), plan, 0, 0}, st);
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((join_up_kernel<FP8>), dim3(join_blocks((int64_t)m * f)), dim3(256), 0, st, part, plan.shares,
-                           sc, gate, up, h, m, f, act);
-        return hipGetLastError();
-    }
-    switch (pick_tile(m, f, ceil_div(d * (FP8 ? 1 : 2), 128), true)) {
+    const Choice c = up_choice(m, d, f, E);
+    switch (c.tile) {
+        case kThin:
+            if constexpr (FP8)
+                return THIN_BY_SIZE(launch_thin_up_fp8, m, d * E, x, wg, wu, sc, gate, up, h, m, d, f, act, st);
+            else
+                return THIN_BY_SIZE(launch_thin_up, m, d * E, x, wg, wu, sc, gate, up, h, m, d, f, act, st);
+        case kSplit: {
+            const hipError_t e = split::launch_partial<C64>({{x, x}, {wg, wu}, part, m, f, d * E, c.plan, 0, 0}, st);
+            if (e != hipSuccess) return e;
+            hipLaunchKernelGGL((join_up_kernel<FP8>), dim3(join_blocks((int64_t)m * f)), dim3(256), 0, st, part,
+                               c.plan.shares, sc, gate, up, h, m, f, act);
+            return hipGetLastError();
+        }
         case kTile256:
             return launch_up_as<Cfg<256, 256, 2, KC, KC, true, false, FP8>>(x, wg, wu, sc, gate, up, h, m, d, f, act, st);
         case kTile128:
@@ -456,28 +443,20 @@ static hipError_t launch_product_as(const uint16_t* a, const uint16_t* a2, const
     return hipGetLastError();
 }
 
-template <bool SEG>
-static split::Plan product_plan(int m, int n, int k) {
-    double unsplit;
-    const int64_t kt = ceil_div(k, 64);
-    pick_tile(m, n, (SEG ? 2 : 1) * kt, false, 1, &unsplit);
-    return split::plan(m, n, kt, SEG ? 2 : 1, false, unsplit);
-}
-
 template <Lay LB, bool SEG, Out O>
 static hipError_t launch_product(const uint16_t* a, const uint16_t* a2, const uint16_t* b, const uint16_t* b2,
                                  uint16_t* c, const GateGrad& gg, float* part, int m, int n, int k, hipStream_t st) {
-    const split::Plan plan = product_plan<SEG>(m, n, k);
-    if (plan.shares > 1) {
-        const hipError_t e =
-            split::launch_partial<Cfg<64, 64, 4, KC, LB>>({{a, a2}, {b, b2}, part, m, n, 2 * k, plan, 0, 0}, st);
-        if (e != hipSuccess) return e;
-        if constexpr (O == STORE) return split::launch_join(part, plan.shares, c, m, n, st);
-        hipLaunchKernelGGL(join_gate_grad_kernel, dim3(join_blocks((int64_t)m * n)), dim3(256), 0, st, part, plan.shares,
-                           gg, (int64_t)m * n);
-        return hipGetLastError();
-    }
-    switch (pick_tile(m, n, (SEG ? 2 : 1) * ceil_div(k, 64), false)) {
+    const Choice ch = product_choice(m, n, k, SEG);
+    switch (ch.tile) {
+        case kSplit: {
+            const hipError_t e =
+                split::launch_partial<Cfg<64, 64, 4, KC, LB>>({{a, a2}, {b, b2}, part, m, n, 2 * k, ch.plan, 0, 0}, st);
+            if (e != hipSuccess) return e;
+            if constexpr (O == STORE) return split::launch_join(part, ch.plan.shares, c, m, n, st);
+            hipLaunchKernelGGL(join_gate_grad_kernel, dim3(join_blocks((int64_t)m * n)), dim3(256), 0, st, part,
+                               ch.plan.shares, gg, (int64_t)m * n);
+            return hipGetLastError();
+        }
         case kTile256: return launch_product_as<Cfg<256, 256, 2, KC, LB, false, SEG>, O>(a, a2, b, b2, c, gg, m, n, k, st);
         case kTile128: return launch_product_as<Cfg<128, 128, 2, KC, LB, false, SEG>, O>(a, a2, b, b2, c, gg, m, n, k, st);
         case kTile128D: return launch_product_as<Cfg<128, 128, 4, KC, LB, false, SEG>, O>(a, a2, b, b2, c, gg, m, n, k, st);
@@ -493,7 +472,7 @@ static hipError_t launch_grads_as(const Grads& p, int m, int d, int f, hipStream
 }
 
 static hipError_t launch_grads(const Grads& p, int m, int d, int f, hipStream_t st) {
-    switch (pick_tile(d, f, ceil_div(m, 64), false, 3)) {
+    switch (grads_choice(m, d, f)) {
         case kTile256: return launch_grads_as<Cfg<256, 256, 2, KR, KR>>(p, m, d, f, st);
         case kTile128: return launch_grads_as<Cfg<128, 128, 2, KR, KR>>(p, m, d, f, st);
         case kTile128D: return launch_grads_as<Cfg<128, 128, 4, KR, KR>>(p, m, d, f, st);
@@ -504,14 +483,7 @@ static hipError_t launch_grads(const Grads& p, int m, int d, int f, hipStream_t 
 // dx = dgate w_gate + dup w_up and the weights' gradients.
 static hipError_t launch_input_and_grads(const Grads& p, const uint16_t* wg, const uint16_t* wu, uint16_t* dx,
                                          float* part, int m, int d, int f, hipStream_t st) {
-    double apart_x, apart_w;
-    pick_tile(m, d, 2 * ceil_div(f, 64), false, 1, &apart_x);
-    pick_tile(d, f, ceil_div(m, 64), false, 3, &apart_w);
-    const double launch = 1.5;  // of a second kernel
-    if (product_plan<true>(m, d, f).shares == 1 &&
-        cost64(ceil_div(m, 64) * ceil_div(d, 64), 2 * ceil_div(f, 64)) +
-                cost64_more(3 * ceil_div(d, 64) * ceil_div(f, 64), ceil_div(m, 64)) <
-            apart_x + apart_w + launch) {
+    if (grads_with_dx(m, d, f)) {
         using CX = Cfg<64, 64, 4, KC, KR, false, true>;
         using CW = Cfg<64, 64, 4, KR, KR>;
         const Product px = product_of<CX>(p.dgate, p.dup, wg, wu, dx, m, d, f);
@@ -540,16 +512,16 @@ using namespace ffn;
 // split product is largest (its products run one after the other).
 static int64_t front_bytes(int64_t arrays, int64_t m, int64_t f) { return (arrays * m * f * 2 + 255) / 256 * 256; }
 
-int64_t gated_up_a8w8_shares_bytes(int m, int d, int f) { return split::bytes(up_plan<true>(m, d, f), m, f, true); }
+int64_t gated_up_a8w8_shares_bytes(int m, int d, int f) { return split::bytes(up_choice(m, d, f, 1).plan, m, f, true); }
 
 int64_t gated_ffn_workspace_bytes(int m, int d, int f) {
-    const int64_t down = m <= kThinMost ? 0 : split::bytes(product_plan<false>(m, d, f), m, d, false);
-    return front_bytes(1, m, f) + larger(split::bytes(up_plan<false>(m, d, f), m, f, true), down);
+    const int64_t down = m <= kThinMost ? 0 : split::bytes(product_choice(m, d, f, false).plan, m, d, false);
+    return front_bytes(1, m, f) + larger(split::bytes(up_choice(m, d, f, 2).plan, m, f, true), down);
 }
 
 int64_t gated_ffn_backward_workspace_bytes(int m, int d, int f) {
-    return front_bytes(3, m, f) + larger(split::bytes(product_plan<false>(m, f, d), m, f, false),
-                                         split::bytes(product_plan<true>(m, d, f), m, d, false));
+    return front_bytes(3, m, f) + larger(split::bytes(product_choice(m, f, d, false).plan, m, f, false),
+                                         split::bytes(product_choice(m, d, f, true).plan, m, d, false));
 }
 
 hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* wg, const uint16_t* wu, const uint16_t* wd,

@@ -396,25 +396,15 @@ __global__ void __launch_bounds__(kThreads) lora_tile_kernel(const uint16_t* xp,
     }
 }
 
-// Shares of the few-token first product: 2 KiB of a row each, kMost at most.
-static int shrink_per(int k) {
-    const int64_t per = larger(2048, ceil_div(ceil_div(2 * (int64_t)k, split::kMost), 128) * 128);
-    return (int)per;
-}
-static int shrink_shares(int k) { return (int)ceil_div(2 * (int64_t)k, shrink_per(k)); }
-
 // MB: up to 64 ranks a workgroup.  base: the shared product too.
 template <int MB>
 static hipError_t launch_shrink_as(Shrink p, const split::Args* base, hipStream_t st) {
     p.groups = (p.m + 15) / 16;
     p.nids = p.adapters < 16 ? p.adapters : 16;
     p.rblocks = (p.r + 16 * MB - 1) / (16 * MB);
-    const int blocks = p.groups * p.nids * p.rblocks * p.shares;
+    const int blocks = shrink_blocks(p.m, p.k, p.r, p.adapters);
     using C = Cfg<64, 64, 4, KC, KC>;
-    // one launch where the first product's workgroups take one place on each
-    // unit at most; more of them are held up by the stages they do not use
-    // (256 tokens x 4096, 32 adapters of rank 16: 52 us against 42)
-    if (base && blocks <= kUnits) {
+    if (base && shrink_with_base(blocks)) {
         split::Args b = *base;
         const int more = split::partial_blocks<C>(b);
         hipLaunchKernelGGL((shrink_and_base_kernel<MB, C>), dim3(blocks + more), dim3(kThreads), 0, st, p, blocks, b);
@@ -426,9 +416,11 @@ static hipError_t launch_shrink_as(Shrink p, const split::Args* base, hipStream_
 }
 
 static hipError_t launch_shrink(const Shrink& p, const split::Args* base, hipStream_t st) {
-    return p.r <= 16   ? launch_shrink_as<1>(p, base, st)
-           : p.r <= 32 ? launch_shrink_as<2>(p, base, st)
-                       : launch_shrink_as<4>(p, base, st);
+    switch (shrink_mb(p.r)) {
+        case 1: return launch_shrink_as<1>(p, base, st);
+        case 2: return launch_shrink_as<2>(p, base, st);
+        default: return launch_shrink_as<4>(p, base, st);
+    }
 }
 
 // A span's rows of `cols` values stay below 2^31 bytes.
@@ -454,9 +446,8 @@ static hipError_t launch_tile(const Second& p, hipStream_t st) {
 }
 
 static hipError_t launch_second(const Second& p, hipStream_t st) {
-    // beside a given c there is little to do per tile, so small tiles, many at once
     if (p.c) return launch_tile<Gathered<64, 64, 2>, false>(p, st);
-    switch (pick_tile(p.m, p.n, ceil_div(p.k, 64), false)) {
+    switch (second_choice(p.m, p.n, p.k)) {
         case kTile256: return launch_tile<Gathered<256, 256, 2>, true>(p, st);
         case kTile128: return launch_tile<Gathered<128, 128, 2>, true>(p, st);
         case kTile128D: return launch_tile<Gathered<128, 128, 4>, true>(p, st);
@@ -466,26 +457,6 @@ static hipError_t launch_second(const Second& p, hipStream_t st) {
 }  // namespace lora
 
 using namespace lora;
-
-constexpr int kJoinMost = 256;  // tokens whose adapters' part is summed value by value
-
-// How the shared product of few tokens is shared out.
-static split::Plan base_plan(int m, int n, int k) {
-    const int64_t kt = ceil_div(k, 64);
-    const double one = (double)ceil_div(ceil_div(m, 64) * ceil_div(n, 64), kUnits) * (2.7 + 0.23 * (double)kt);
-    return split::plan(m, n, kt, 1, false, one);
-}
-
-// How the first product of many tokens is shared out: two workgroups a unit,
-// four K tiles at least to a share.
-static split::Plan shrink_plan(int m, int k, int r) {
-    const int64_t kt = ceil_div(k, 64), tiles = ceil_div(m, 64) * ceil_div(r, 64);
-    int64_t s = 2 * kUnits / tiles;
-    s = s > kt / 4 ? kt / 4 : s;
-    s = s < 1 ? 1 : s > split::kMost ? split::kMost : s;
-    const int64_t per = ceil_div(kt, s);
-    return split::Plan{(int)ceil_div(kt, per), (int)per, 1};
-}
 
 // Workspace: few tokens, v's shares and the shared product's; many, v in bf16,
 // the tokens' order (row of the span and id), and v's shares.

@@ -1,10 +1,8 @@
 // split.h -- products with few output tiles and a long K, gfx950: K is split
 // over workgroups as well, each writes its share of the sums as fp32, and a
 // second kernel adds the shares in order and finishes the values.  The shares
-// are joined in a fixed order, so results do not depend on timing.
-//
-// Worth it where the tiles alone would leave most compute units idle: at 64 x
-// 7168 -> 2 x 2048 columns there are 32 tiles of 112 K tiles each for 256 units.
+// are joined in a fixed order, so results do not depend on timing.  How K is
+// shared: dense_pick.h.
 #pragma once
 #include "dense_core.h"
 #include "dense_pick.h"
@@ -12,32 +10,6 @@
 namespace dmm {
 namespace split {
 using namespace dense;
-
-constexpr int kMost = 16;  // shares of one output value
-
-// How K is shared: `per` K tiles to a share, `shares` shares in all; with two
-// segments (a b + a2 b2) the first half of the shares takes the first product.
-struct Plan {
-    int shares, per, segs;
-};
-
-// The plan for rows x cols outputs over kt K tiles (of each segment), or shares
-// = 1 where no split pays.  Model as in pick_tile: the tiles' round, the shares'
-// way to memory and back, and a second launch.
-inline Plan plan(int64_t rows, int64_t cols, int64_t kt, int segs, bool gated, double unsplit) {
-    const int64_t cus = kUnits, tiles = ceil_div(rows, 64) * ceil_div(cols, 64);
-    Plan best{1, (int)kt, segs};
-    double c = unsplit;
-    for (int64_t s = 2 / segs; s * segs <= kMost; ++s) {
-        if (s * segs < 2) continue;
-        const int64_t per = ceil_div(kt, s), n = ceil_div(kt, per) * segs;
-        if (per < 4 || n < 2) break;
-        const double round = (double)ceil_div(tiles * n, cus) * (2.7 + (gated ? 0.27 : 0.23) * (double)per);
-        const double t = round + 4.0 + (double)(n * rows * cols * (gated ? 2 : 1)) * 8e-6 / 4.0;
-        if (t < c) best = Plan{(int)n, (int)per, segs}, c = t;
-    }
-    return best;
-}
 
 struct Args {
     const void* a[2];  // one per segment
@@ -139,10 +111,6 @@ __global__ void __launch_bounds__(256) join_kernel(const float* part, int shares
 inline hipError_t launch_join(const float* part, int shares, uint16_t* y, int64_t m, int64_t n, hipStream_t st) {
     hipLaunchKernelGGL((join_kernel<>), dim3((unsigned)ceil_div(m * n, 2048)), dim3(256), 0, st, part, shares, y, m * n);
     return hipGetLastError();
-}
-
-inline int64_t bytes(const Plan& p, int64_t m, int64_t n, bool gated) {
-    return p.shares < 2 ? 0 : (int64_t)p.shares * m * n * (gated ? 8 : 4);
 }
 
 }  // namespace split

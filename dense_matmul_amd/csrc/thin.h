@@ -10,6 +10,7 @@
 // wave order, so the result does not depend on timing.
 #pragma once
 #include "common.h"
+#include "dense_pick.h"
 
 namespace dmm {
 namespace thin {
@@ -104,9 +105,6 @@ struct Join {
         return s;
     }
 };
-
-// Waves for a row of kb bytes: two units or more each.
-constexpr int waves_for(int kb) { return kb >= 4096 ? 16 : kb >= 2048 ? 8 : 4; }
 
 __device__ __forceinline__ uint16_t to_bf16(float v) { return (uint16_t)(pack_bf16(v, 0.f) & 0xffff); }
 
