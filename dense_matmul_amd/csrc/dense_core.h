@@ -59,7 +59,6 @@ struct Mat {
     int rows;
 };
 
-// The share of one wave in the DMAs of one operand's stages.
 // The share of one wave in the DMAs of one operand's stages.  SEG: K runs over
 // two matrices of one shape, one after the other.
 template <Lay L, int ROWS, bool SEG, bool GATHER = false>

@@ -272,20 +272,17 @@ __global__ void __launch_bounds__(kThreads) input_and_weight_grad_kernel(Product
         weight_grad_body<CW>(ring, p, m, d, f, td, tf, order::xcd_list(blockIdx.x - first, 3 * td * tf, 3 * td * tf).first);
 }
 
-// Few tokens (at most 16 MB): eight columns of h per workgroup, whose 16
-// weight rows are the eight gate rows and the eight up rows.
-template <bool FP8, int MB, int WAVES>
+// At most 16 tokens: eight columns of h per workgroup, whose 16 weight rows are
+// the eight gate rows and the eight up rows.
+template <bool FP8, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES) thin_up_kernel(const char* xp, const char* wg, const char* wu, Scales sc,
                                                              uint16_t* gate, uint16_t* up, uint16_t* h, int m, int d,
                                                              int f, int act) {
-    __shared__ thin::Join<MB, WAVES> join;
+    __shared__ thin::Join<1, WAVES> join;
     const int i = lane_id() & 15, n0 = blockIdx.x * 8, kb = FP8 ? d : 2 * d;
-    const char* xrow[MB];
-#pragma unroll
-    for (int b = 0; b < MB; ++b) xrow[b] = xp + (int64_t)(16 * b + i < m ? 16 * b + i : m - 1) * kb;
-    v4f acc[MB];
-    const char* wrow[1] = {(i < 8 ? wg : wu) + (int64_t)(n0 + (i & 7)) * kb};
-    thin::product<FP8, 1, MB, WAVES>(wrow, xrow, kb, acc);
+    const char* xrow[1] = {xp + (int64_t)(i < m ? i : m - 1) * kb};
+    v4f acc[1];
+    thin::product<FP8, 1, WAVES>((i < 8 ? wg : wu) + (int64_t)(n0 + (i & 7)) * kb, xrow, kb, acc);
     join.put(acc);
     for (int e = threadIdx.x; e < 8 * m; e += 64 * WAVES) {
         const int r = e >> 3, c = e & 7;
@@ -303,18 +300,16 @@ __global__ void __launch_bounds__(64 * WAVES) thin_up_kernel(const char* xp, con
     }
 }
 
-// y [m, n] = a [m, k] b [n, k]^T for few rows of a: 16 columns per workgroup.
-template <int MB, int WAVES>
+// y [m, n] = a [m, k] b [n, k]^T for at most 16 rows of a: 16 columns per
+// workgroup.
+template <int WAVES>
 __global__ void __launch_bounds__(64 * WAVES) thin_product_kernel(const uint16_t* a, const uint16_t* b, uint16_t* y,
                                                                   int m, int n, int k) {
-    __shared__ thin::Join<MB, WAVES> join;
+    __shared__ thin::Join<1, WAVES> join;
     const int i = lane_id() & 15, n0 = blockIdx.x * 16;
-    const char* xrow[MB];
-#pragma unroll
-    for (int q = 0; q < MB; ++q) xrow[q] = (const char*)(a + (int64_t)(16 * q + i < m ? 16 * q + i : m - 1) * k);
-    v4f acc[MB];
-    const char* wrow[1] = {(const char*)(b + (int64_t)(n0 + i < n ? n0 + i : n - 1) * k)};
-    thin::product<false, 1, MB, WAVES>(wrow, xrow, k * 2, acc);
+    const char* xrow[1] = {(const char*)(a + (int64_t)(i < m ? i : m - 1) * k)};
+    v4f acc[1];
+    thin::product<false, 1, WAVES>((const char*)(b + (int64_t)(n0 + i < n ? n0 + i : n - 1) * k), xrow, k * 2, acc);
     join.put(acc);
     for (int e = threadIdx.x; e < 16 * m; e += 64 * WAVES) {
         const int r = e >> 4, c = e & 15;
@@ -350,6 +345,15 @@ __global__ void __launch_bounds__(256) join_up_kernel(const float* part, int sha
     }
 }
 
+// y from the shares of a product.
+__global__ void __launch_bounds__(256) join_kernel(const float* part, int shares, uint16_t* y, int64_t values) {
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (at >= values) return;
+    float v[8];
+    split::sum8(part, shares, values, at, v);
+    *(v4i*)(y + at) = pack8(v);
+}
+
 // dgate, dup and h from the shares of dh.
 __global__ void __launch_bounds__(256) join_gate_grad_kernel(const float* part, int shares, GateGrad gg, int64_t values) {
     const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
@@ -375,20 +379,20 @@ __global__ void __launch_bounds__(256) join_gate_grad_kernel(const float* part, 
 
 static unsigned join_blocks(int64_t values) { return (unsigned)ceil_div(values, 2048); }
 
-template <bool FP8, int MB, int WAVES>
+template <bool FP8, int WAVES>
 static hipError_t launch_thin_up_any(const void* x, const void* wg, const void* wu, const Scales& sc, uint16_t* gate,
                                      uint16_t* up, uint16_t* h, int m, int d, int f, int act, hipStream_t st) {
-    hipLaunchKernelGGL((thin_up_kernel<FP8, MB, WAVES>), dim3(f / 8), dim3(64 * WAVES), 0, st, (const char*)x,
+    hipLaunchKernelGGL((thin_up_kernel<FP8, WAVES>), dim3(f / 8), dim3(64 * WAVES), 0, st, (const char*)x,
                        (const char*)wg, (const char*)wu, sc, gate, up, h, m, d, f, act);
     return hipGetLastError();
 }
-template <int MB, int WAVES, class... A>
+template <int WAVES, class... A>
 static hipError_t launch_thin_up(A... a) {
-    return launch_thin_up_any<false, MB, WAVES>(a...);
+    return launch_thin_up_any<false, WAVES>(a...);
 }
-template <int MB, int WAVES, class... A>
+template <int WAVES, class... A>
 static hipError_t launch_thin_up_fp8(A... a) {
-    return launch_thin_up_any<true, MB, WAVES>(a...);
+    return launch_thin_up_any<true, WAVES>(a...);
 }
 template <class C>
 static hipError_t launch_up_as(const void* x, const void* wg, const void* wu, const Scales& sc, uint16_t* gate,
@@ -409,9 +413,9 @@ static hipError_t launch_up(const void* x, const void* wg, const void* wu, const
     switch (c.tile) {
         case kThin:
             if constexpr (FP8)
-                return THIN_BY_SIZE(launch_thin_up_fp8, m, d * E, x, wg, wu, sc, gate, up, h, m, d, f, act, st);
+                return THIN_BY_SIZE(launch_thin_up_fp8, d * E, x, wg, wu, sc, gate, up, h, m, d, f, act, st);
             else
-                return THIN_BY_SIZE(launch_thin_up, m, d * E, x, wg, wu, sc, gate, up, h, m, d, f, act, st);
+                return THIN_BY_SIZE(launch_thin_up, d * E, x, wg, wu, sc, gate, up, h, m, d, f, act, st);
         case kSplit: {
             const hipError_t e = split::launch_partial<C64>({{x, x}, {wg, wu}, part, m, f, d * E, c.plan, 0, 0}, st);
             if (e != hipSuccess) return e;
@@ -452,9 +456,12 @@ static hipError_t launch_product(const uint16_t* a, const uint16_t* a2, const ui
             const hipError_t e =
                 split::launch_partial<Cfg<64, 64, 4, KC, LB>>({{a, a2}, {b, b2}, part, m, n, 2 * k, ch.plan, 0, 0}, st);
             if (e != hipSuccess) return e;
-            if constexpr (O == STORE) return split::launch_join(part, ch.plan.shares, c, m, n, st);
-            hipLaunchKernelGGL(join_gate_grad_kernel, dim3(join_blocks((int64_t)m * n)), dim3(256), 0, st, part,
-                               ch.plan.shares, gg, (int64_t)m * n);
+            const int64_t values = (int64_t)m * n;
+            if constexpr (O == STORE)
+                hipLaunchKernelGGL(join_kernel, dim3(join_blocks(values)), dim3(256), 0, st, part, ch.plan.shares, c, values);
+            else
+                hipLaunchKernelGGL(join_gate_grad_kernel, dim3(join_blocks(values)), dim3(256), 0, st, part,
+                                   ch.plan.shares, gg, values);
             return hipGetLastError();
         }
         case kTile256: return launch_product_as<Cfg<256, 256, 2, KC, LB, false, SEG>, O>(a, a2, b, b2, c, gg, m, n, k, st);
@@ -497,10 +504,10 @@ static hipError_t launch_input_and_grads(const Grads& p, const uint16_t* wg, con
     return e != hipSuccess ? e : launch_grads(p, m, d, f, st);
 }
 
-template <int MB, int WAVES>
+template <int WAVES>
 static hipError_t launch_thin_product(const uint16_t* a, const uint16_t* b, uint16_t* y, int m, int n, int k,
                                       hipStream_t st) {
-    hipLaunchKernelGGL((thin_product_kernel<MB, WAVES>), dim3((n + 15) / 16), dim3(64 * WAVES), 0, st, a, b, y, m, n,
+    hipLaunchKernelGGL((thin_product_kernel<WAVES>), dim3((n + 15) / 16), dim3(64 * WAVES), 0, st, a, b, y, m, n,
                        k);
     return hipGetLastError();
 }
@@ -531,7 +538,7 @@ hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* wg, const uint16_
     float* part = (float*)((char*)ws + front_bytes(1, m, f));
     const hipError_t e = launch_up<false>(x, wg, wu, Scales{}, gate, up, h, part, m, d, f, act, st);
     if (e != hipSuccess) return e;
-    if (m <= kThinMost) return THIN_BY_SIZE(launch_thin_product, m, f * 2, h, wd, y, m, d, f, st);
+    if (m <= kThinMost) return THIN_BY_SIZE(launch_thin_product, f * 2, h, wd, y, m, d, f, st);
     return launch_product<KC, false, STORE>(h, nullptr, wd, nullptr, y, GateGrad{}, part, m, d, f, st);
 }
 

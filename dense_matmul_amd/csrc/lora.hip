@@ -63,8 +63,8 @@ struct Shrink {
     const int* ids;
     float* part;
     int m, k, r, adapters;
-    int per, shares;             // bytes of K to a share
-    int groups, nids, rblocks;   // 16 tokens; ids of a group; 16 MB ranks
+    int per, shares;      // bytes of K to a share
+    int groups, rblocks;  // 16 tokens; 16 MB ranks
 };
 constexpr int kWaves = kThreads / 64;
 
@@ -79,14 +79,14 @@ __device__ __forceinline__ void shrink_body(thin::Join<MB, kWaves>& join, const 
     const int64_t from = (int64_t)share * p.per;
     const int kb = 2 * p.k - from < p.per ? (int)(2 * p.k - from) : p.per;
     const char* mat = (const char*)(p.a + ((int64_t)cur * p.r + r0) * p.k) + from;
-    const char *rows[MB], *toks[1];
+    const char* rows[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) rows[b] = mat + (int64_t)(r0 + 16 * b + i < p.r ? 16 * b + i : 0) * (2 * p.k);
     // a token of another id has this id's first stand in for it, whose row the L1 holds
     const int row = t0 + (mine == cur ? i : (int)__builtin_ctzll(__ballot(mine == cur)));
-    toks[0] = (const char*)(p.x + (int64_t)(row < p.m ? row : p.m - 1) * p.k) + from;
+    const char* tok = (const char*)(p.x + (int64_t)(row < p.m ? row : p.m - 1) * p.k) + from;
     v4f acc[MB];
-    thin::product<false, 1, MB, kWaves>(toks, rows, kb, acc);
+    thin::product<false, MB, kWaves>(tok, rows, kb, acc);
     join.put(acc);
     const int width = p.r - r0 < 16 * MB ? p.r - r0 : 16 * MB;
     for (int e = threadIdx.x; e < 16 * width; e += kThreads) {
@@ -400,7 +400,6 @@ __global__ void __launch_bounds__(kThreads) lora_tile_kernel(const uint16_t* xp,
 template <int MB>
 static hipError_t launch_shrink_as(Shrink p, const split::Args* base, hipStream_t st) {
     p.groups = (p.m + 15) / 16;
-    p.nids = p.adapters < 16 ? p.adapters : 16;
     p.rblocks = (p.r + 16 * MB - 1) / (16 * MB);
     const int blocks = shrink_blocks(p.m, p.k, p.r, p.adapters);
     using C = Cfg<64, 64, 4, KC, KC>;
@@ -478,7 +477,7 @@ hipError_t launch_lora(const uint16_t* x, const uint16_t* w, const uint16_t* c, 
         float* v = (float*)ws;
         const split::Plan plan = c ? split::Plan{0, 0, 1} : base_plan(m, n, k);
         const split::Args base{{x, x}, {w, w}, part, m, n, 2 * k, plan, 0, 0};
-        e = launch_shrink(Shrink{x, a, ids, v, m, k, r, adapters, shrink_per(k), shrink_shares(k), 0, 0, 0},
+        e = launch_shrink(Shrink{x, a, ids, v, m, k, r, adapters, shrink_per(k), shrink_shares(k), 0, 0},
                           c ? nullptr : &base, st);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(join_lora_kernel, dim3((n + 255) / 256, m), dim3(256), 0, st, part, plan.shares, v,

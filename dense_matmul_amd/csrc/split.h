@@ -99,19 +99,5 @@ __device__ __forceinline__ void sum8(const float* part, int shares, int64_t stri
     }
 }
 
-// y [m, n] bf16 = the sum of the shares.
-template <int DUMMY = 0>
-__global__ void __launch_bounds__(256) join_kernel(const float* part, int shares, uint16_t* y, int64_t values) {
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-    if (at >= values) return;
-    float v[8];
-    sum8(part, shares, values, at, v);
-    *(v4i*)(y + at) = pack8(v);
-}
-inline hipError_t launch_join(const float* part, int shares, uint16_t* y, int64_t m, int64_t n, hipStream_t st) {
-    hipLaunchKernelGGL((join_kernel<>), dim3((unsigned)ceil_div(m * n, 2048)), dim3(256), 0, st, part, shares, y, m * n);
-    return hipGetLastError();
-}
-
 }  // namespace split
 }  // namespace dmm

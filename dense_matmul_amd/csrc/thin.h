@@ -1,10 +1,11 @@
-// thin.h -- products of few tokens with a weight, gfx950: at most 16 MB rows
-// x [m, k] against 16 TB weight rows per workgroup, K split over its waves.
+// thin.h -- products of few rows, gfx950: 16 streamed rows (a weight's, or for
+// the adapters the tokens) against 16 MB rows of the other operand x per
+// workgroup, K split over its waves.
 //
-// Such a product is bound by reading the weight once, so the weight goes
+// Such a product is bound by reading the streamed rows once, so they go
 // straight from memory to the matrix op's registers (no LDS: no wave uses
-// another's weights) and every wave keeps all of its K share's loads in
-// flight: lane (i, g) = (l % 16, l / 16) reads 16 bytes of weight row i, four
+// another's) and every wave keeps all of its K share's loads in
+// flight: lane (i, g) = (l % 16, l / 16) reads 16 bytes of streamed row i, four
 // lanes a 64-byte run, two such steps a 128-byte unit.  x comes from the L2 in
 // the same shape.  The waves' partial products meet in LDS and are summed in
 // wave order, so the result does not depend on timing.
@@ -32,28 +33,24 @@ __device__ __forceinline__ v4f matrix_op(bool fp8, v4i w, v4i x, v4f c) {
 #endif
 }
 
-// acc[MB t + b]: this wave's share of x rows 16 b .. times weight rows 16 t ..;
-// lane (i, g) ends with x row 16 b + i, weight rows 16 t + 4 g .. + 3.  wrow
-// and xrow are the lane's rows (any valid row where there is none: such
-// outputs are not used), kb the bytes of a row, a multiple of 16.
-template <bool FP8, int TB, int MB, int WAVES>
-__device__ __forceinline__ void product(const char* const (&wrow)[TB], const char* const (&xrow)[MB], int kb,
-                                        v4f (&acc)[TB * MB]) {
-    constexpr int UN = TB + MB <= 2 ? 4 : TB + MB <= 5 ? 2 : 1;  // 128-byte units in flight
+// acc[b]: this wave's share of x rows 16 b .. times the streamed rows; lane
+// (i, g) ends with x row 16 b + i, streamed rows 4 g .. + 3.  wrow and xrow are
+// the lane's rows (any valid row where there is none: such outputs are not
+// used), kb the bytes of a row, a multiple of 16.
+template <bool FP8, int MB, int WAVES>
+__device__ __forceinline__ void product(const char* wrow, const char* const (&xrow)[MB], int kb, v4f (&acc)[MB]) {
+    constexpr int UN = MB == 1 ? 4 : 2;  // 128-byte units in flight
     const int lane = lane_id(), w = wave_id(), at = 16 * (lane >> 4);
     const int units = (kb + 127) / 128, per = (units + WAVES - 1) / WAVES;
     const int lo = w * per, end = lo + per < units ? lo + per : units, whole = kb / 128;
     const int full = end < whole ? end : whole;
 #pragma unroll
-    for (int b = 0; b < TB * MB; ++b) acc[b] = (v4f){0.f, 0.f, 0.f, 0.f};
+    for (int b = 0; b < MB; ++b) acc[b] = (v4f){0.f, 0.f, 0.f, 0.f};
     int u = lo;
     for (; u + UN <= full; u += UN) {
-        v4i wv[TB][2 * UN], xv[MB][2 * UN];
+        v4i wv[2 * UN], xv[MB][2 * UN];
 #pragma unroll
-        for (int t = 0; t < TB; ++t)
-#pragma unroll
-            for (int s = 0; s < 2 * UN; ++s)
-                wv[t][s] = __builtin_nontemporal_load((const v4i*)(wrow[t] + u * 128 + 64 * s + at));
+        for (int s = 0; s < 2 * UN; ++s) wv[s] = __builtin_nontemporal_load((const v4i*)(wrow + u * 128 + 64 * s + at));
 #pragma unroll
         for (int b = 0; b < MB; ++b)
 #pragma unroll
@@ -61,9 +58,7 @@ __device__ __forceinline__ void product(const char* const (&wrow)[TB], const cha
 #pragma unroll
         for (int s = 0; s < 2 * UN; ++s)
 #pragma unroll
-            for (int t = 0; t < TB; ++t)
-#pragma unroll
-                for (int b = 0; b < MB; ++b) acc[MB * t + b] = matrix_op(FP8, wv[t][s], xv[b][s], acc[MB * t + b]);
+            for (int b = 0; b < MB; ++b) acc[b] = matrix_op(FP8, wv[s], xv[b][s], acc[b]);
     }
     // what is left of the share, the row's last partial unit included: both
     // operands are zero past the row's end
@@ -73,23 +68,18 @@ __device__ __forceinline__ void product(const char* const (&wrow)[TB], const cha
             const int off = u * 128 + 64 * s + at;
             const bool in = off < kb;
             const int from = in ? off : 0;
-            v4i wv[TB];
-#pragma unroll
-            for (int t = 0; t < TB; ++t) {
-                wv[t] = *(const v4i*)(wrow[t] + from);
-                if (!in) wv[t] = (v4i){0, 0, 0, 0};
-            }
+            v4i wv = *(const v4i*)(wrow + from);
+            if (!in) wv = (v4i){0, 0, 0, 0};
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
                 v4i xv = *(const v4i*)(xrow[b] + from);
                 if (!in) xv = (v4i){0, 0, 0, 0};
-#pragma unroll
-                for (int t = 0; t < TB; ++t) acc[MB * t + b] = matrix_op(FP8, wv[t], xv, acc[MB * t + b]);
+                acc[b] = matrix_op(FP8, wv, xv, acc[b]);
             }
         }
 }
 
-// The waves' shares in LDS, and the sum over them of x row r, weight row n.
+// The waves' shares in LDS, and the sum over them of x row r, streamed row n.
 template <int MB, int WAVES>
 struct Join {
     v4f part[WAVES][MB][64];
@@ -111,8 +101,8 @@ __device__ __forceinline__ uint16_t to_bf16(float v) { return (uint16_t)(pack_bf
 }  // namespace thin
 }  // namespace dmm
 
-// F<MB, WAVES> for at most 16 rows of kb bytes
-#define THIN_BY_SIZE(F, m, kb, ...)                     \
-    (thin::waves_for(kb) == 16  ? F<1, 16>(__VA_ARGS__) \
-     : thin::waves_for(kb) == 8 ? F<1, 8>(__VA_ARGS__)  \
-                                : F<1, 4>(__VA_ARGS__))
+// F<WAVES> for rows of kb bytes
+#define THIN_BY_SIZE(F, kb, ...)                     \
+    (thin::waves_for(kb) == 16  ? F<16>(__VA_ARGS__) \
+     : thin::waves_for(kb) == 8 ? F<8>(__VA_ARGS__)  \
+                                : F<4>(__VA_ARGS__))
