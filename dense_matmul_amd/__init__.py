@@ -28,6 +28,10 @@ Functions (names as in the C ABI):
     lora_gemm_bf16(x, w, lora_a, lora_b, adapter_ids, scales, out=None)  -> bf16 [M,N]
     lora_add_bf16(c, x, lora_a, lora_b, adapter_ids, scales, out=None)   -> bf16 [M,N]
 
+No call records a gradient: results are detached from inputs that require one,
+and training calls layer_norm_backward and gated_ffn_backward itself, as
+examples/ffn_sublayer.py does.
+
 Argument errors (status DMM_EINVAL) raise ValueError; everything else raises
 RuntimeError.
 """

@@ -57,11 +57,11 @@ constexpr int kr_read(int row0, int q, int i, int g, int rows) {
 // unit busy for 16 cycles (32 in fp8), the issue of up to three other
 // instructions fits in there, and a run of them leaves the unit idle.  The
 // DMAs are spread widest: the path from the L1 into LDS moves 64 bytes a
-// cycle, so a K tile of the 256 x 256 shape takes half a step.  Spread over
-// five eighths of a step, the forward and backward passes of the feed-forward
-// block at 16384 x 7168 x 2048 take 1122 and 2219 us, over half 1140 and 2264,
-// over three eighths 1171 and 2335; eleven sixteenths, or the barrier an
-// eighth of a step later, are within 1 % of the first.
+// cycle, so a K tile of the 256 x 256 shape takes half a step.  Against
+// a spread over five eighths of a step, timed in turn, the forward and backward
+// passes of the feed-forward block at 16384 x 7168 x 2048 take 1.6 and 2.0 % more
+// with one over half, 4.4 and 5.2 % over three eighths; eleven sixteenths, or the
+// barrier an eighth of a step later, are within 1 %.
 template <int T, int FIRST, int SECOND, int DMAS>
 struct Plan {
     static constexpr int kMid = T * 9 / 32;  // the wait and the barrier come before matrix op kMid

@@ -3,17 +3,20 @@
 //   dh = dy Wd, dg = dh u act'(g), du = dh act(g), dWd = dy^T h,
 //   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x
 // x, y [m, d]; Wg, Wu [f, d]; Wd [d, f]; all bf16, sums in fp32.  h, dg and du
-// are rounded to bf16 once, as operands of the products that follow.
+// are rounded to bf16 once, as operands of the products that follow: the
+// matrix op of the full rate takes 16-bit operands.  Relative error in the mean
+// square against 64 bits 0.0022-0.0024, where one rounding of the result alone
+// gives 0.0017.
 //
 // Many tokens are bound by the matrix cores: 6 m d f operations forward, 12 m d
 // f backward, which the tile engine takes in two launches and three (dh with
 // its gradients through the activation in the epilogue; dx over both pairs in
 // one sum; the three weight gradients together, none through a transposed
-// copy).  Measured at 16384 x 7168 x 2048: forward 1071 us (1.35
-// PFLOP/s), backward 2241 (1.29), the matrix unit 66-74 % busy at the 1.5-1.8
-// GHz that the part's power allows.  Up to 16 tokens are bound by reading the
-// weights once: one token of 7168 x 2048 takes 14 + 7 us in two launches (4.2
-// TB/s).
+// copy).  Measured at 16384 x 7168 x 2048: forward with gate and up kept
+// 1040-1058 us (1.36-1.39 PFLOP/s), backward 2193-2207 (1.31), the matrix unit
+// 63-72 % busy at the 1.6-1.9 GHz that the part's power allows.  Up to 16 tokens
+// are bound by reading the weights once: one token of 7168 x 2048 takes 14 + 7 us
+// in two launches (4.3 TB/s); 64 tokens, K shared out, 14 + 4 + 8.
 #include "dense_core.h"
 #include "dense_pick.h"
 #include "split.h"
@@ -25,9 +28,9 @@ using namespace dense;
 
 enum Act { SILU = 0, GELU = 1 };
 
-// Results that this call does not read again bypass the caches (nt sc1): the
-// forward pass of 16384 x 7168 x 2048 with gate and up kept takes 1118 us
-// against 1142, the backward pass the same. What the next product reads (h,
+// Results that this call does not read again bypass the caches (nt sc1): timed in
+// turn, the forward pass of 16384 x 7168 x 2048 with gate and up kept takes 2.1 %
+// more without, the backward pass the same.  What the next product reads (h,
 // dgate, dup) does not: 1.5 % slower backward.
 constexpr int kStream = 2 | 16;
 

@@ -17,11 +17,16 @@
 // and no others, and what v holds for a token without an adapter is never
 // used.
 //
+// Rounding v costs little: relative error in the mean square against 64 bits
+// 0.0019-0.0020, where the result's own rounding gives 0.0017 (few tokens: that).
+//
 // Bound by the shared product's operations for many tokens: 8192 x 7168 -> 2048,
-// 16 adapters of rank 64 in runs, 36 us for v's shares, 5 for their join and
-// 179-189 for the product (1.32 PFLOP/s).  Few tokens read every weight once: 48 x
-// 4096 -> 4096, 32 adapters of rank 16, 10 + 4 us.  Beside a given c, 2041 x
-// 1792 -> 1168, rank 40: 7 + 4 + 7 us, three launches' latency.
+// 8 adapters of rank 64 in runs, 37 us for v's shares, 5 for their join and
+// 180-201 for the product (1.21-1.35 PFLOP/s).  Few tokens read every weight
+// once: 48 x 4096 -> 4096, 32 adapters of rank 16, 10 + 4 us.  Beside a given c,
+// 2041 x 1792 -> 1168, 5 adapters of rank 40: 7.5 + 4 + 6.6 us, three launches'
+// latency.  Between the two, and with many ids to a tile, it is passes over ids
+// that cost: 512 x 4096 -> 4096, 32 adapters of rank 16, 24 + 5 + 50 us.
 #include "dense_core.h"
 #include "dense_pick.h"
 #include "split.h"
@@ -177,12 +182,12 @@ __device__ __forceinline__ int next_id(int mine, int cur, int* slot) {
 // so that a tile meets few ids either way (every id of a tile costs a pass).
 // A bitonic sort of id and place in LDS, by each workgroup of the first product
 // for itself; the second product takes the order from memory and its rows of x
-// and v by it (an offset per load and lane, 1-2 % of a call in runs).  8192
+// and v by it (an offset per load and lane, about 2 % of a call in runs).  8192
 // tokens in any order over 128 adapters of rank 64 at 7168 -> 2048 take
-// 346 us beside a given c and 692 with the shared product, and took 1779 and
-// 2402 unsorted (in runs: 116 and 287); 512 over 32 of rank 16 at 4096 -> 4096
-// 37 and 75, 97 and 154.  Which it is depends on
-// the span's ids alone, and a token's result not on its place in a tile.
+// 343 us beside a given c and 683 with the shared product, and took 1779 and
+// 2402 unsorted (in 256 runs: 168 and 384); 512 over 32 of rank 16 at 4096 ->
+// 4096 36 and 76, and took 97 and 154.  Which it is depends on the span's ids
+// alone, and a token's result not on its place in a tile.
 constexpr int kSpan = 1024;
 constexpr int kRuns = 32;  // groups of four consecutive tokens with a change of id, at most, unsorted
 

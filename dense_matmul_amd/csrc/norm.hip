@@ -16,9 +16,11 @@
 // partials in a caller's workspace and then a sum over them in order, so the
 // result does not depend on timing.
 //
-// Measured on one MI355X: forward 32768 x 7168 bf16 185 us, 5.1 TB/s of the
-// bytes that must move (a 4 GiB copy: 4.8); backward 16384 x 7168 140 us, 5.0
-// TB/s; 16 x 1024 forward 6 us, a launch and one row's latency.
+// Measured on one MI355X: forward 32768 x 7168 bf16 184 us, 5.1 TB/s of the
+// bytes that must move (a 4 GiB copy: 4.7-4.8), the same with mean and rstd
+// kept; fp32 16384 x 7168 179 us; backward 16384 x 7168 bf16 139 us, 5.1 TB/s,
+// fp32 266 us, 5.3; 16 x 1024 forward 6 us, a launch and one row's latency; 1117 x
+// 1160 fp32 backward 8 + 3 us, a few rows a wave and then the join's latency.
 #include "common.h"
 
 namespace dmm {

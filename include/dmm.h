@@ -292,7 +292,8 @@ dmm_status gated_ffn_backward_bf16(const uint16_t* dy, const uint16_t* x, const 
 /* The first half of the block over fp8 operands with the scales of
  * gemm_a8w8_ptpc (one per token, one per output channel):
  *   g[m, f] = a_scale[m] gate_scale[f] sum_d A[m, d] Wg[f, d],  u likewise,
- *   h = bf16(act(g) u).
+ *   h = bf16(act(g) u),
+ * the sum times a_scale first, then times the channel's scale, as there.
  * a [m, d], w_gate and w_up [f, d] are E4M3 codes in row order, as
  * quantize_per_token writes them (not preshuffled).  h [m, f] is what
  * quantize_per_token_bf16 takes for the down projection.  workspace:
@@ -312,9 +313,10 @@ dmm_status gated_up_a8w8_ptpc(const uint8_t* a, const uint8_t* w_gate, const uin
  * (a request's tokens repeat its id); scales [adapters] fp32.  An id outside
  * [0, adapters) names no adapter: that token gets the shared part alone.  An
  * adapter's values (infinities and NaN too) reach its own tokens only.  The
- * value scales[i] x[t] lora_a[i]^T is rounded to bf16 at most once, as the
- * operand of the second product; the two parts are summed in fp32 and rounded
- * once.
+ * value scales[i] x[t] lora_a[i]^T stays in fp32 for up to 256 tokens and is
+ * rounded to bf16 once beyond, as the operand of the second product; the two
+ * parts are summed in fp32 and rounded once.  So a token's last bits may depend
+ * on how many tokens the call has, not on their order or on each other.
  * workspace: overwritten, at least lora_gemm_workspace(m, n, k, r) bytes (-1
  * if the sizes break a rule).
  * Rules: m >= 0; n and k positive multiples of 8; r a multiple of 8 up to
