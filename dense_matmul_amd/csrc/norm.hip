@@ -134,7 +134,9 @@ __global__ void __launch_bounds__(NT) forward_kernel(const T* x, const T* w, con
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[0] += xv[i][e];
         row_sum<TPR>(s, slots[0][sub]);
-        const float mu = s[0] * inv;
+        // divided: the reciprocal's rounding would leave a row of one value off its
+        // mean by a last place, and rstd is 1 / sqrt(eps) there
+        const float mu = s[0] / (float)cols;
         s[0] = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
